@@ -35,8 +35,8 @@
 // norm).  What is fp32 (S, R, V' and T) is scaled per row by a power of two to below 2^15 and
 // split into two FP16 terms, hi + lo = the value to 2^-22 of it, or 2^-39 of its row's largest:
 // S K^T and V'' K take 2 products, T R takes 3 (lo x lo, below 2^-22, is dropped).  The two
-// products that only reach the BF16 output, S Q^T and P V', take one term (11 bits against the
-// output's 8).  (Three BF16 terms, 24 bits without any scaling, took 6 + 3 + 3 + 2 + 3 products
+// products that only reach the BF16 output, S Q^T and P V', take one term of S, P and V', rounded to
+// nearest: 2^-11 of each, without a lean, against the output's own 2^-8.  (Three BF16 terms, 24 bits without any scaling, took 6 + 3 + 3 + 2 + 3 products
 // for these 3 + 2 + 2 + 1 + 1.)  The state itself is held in fp32 registers and updated there, so the
 // tensor cores' sums never run longer than one chunk.  b is a pair of floats, so that b_i - b_j is
 // good to fp32 even when b itself is large.
@@ -238,15 +238,20 @@ __device__ __forceinline__ void gc_stored(uint64_t* bar) {
 }
 
 // A pair's FP16 terms: the values with their low 13 mantissa bits cut off (exact in FP16 while
-// normal) and the exact remainder, rounded.
+// normal) and the exact remainder, rounded.  ROUND: the values rounded to nearest and the remainder, for S:
+// S Q^T takes the first term alone, and where a query meets its key all its terms have one sign, so a cut
+// would shrink the outputs by about 2^-11 (8192 x 48: 340.1 us; 339.2 with the cut, 341.9 with every split
+// rounded).
 __device__ __forceinline__ uint32_t gc_half2(float2 v) {
     const __half2 h = __floats2half2_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+template <bool ROUND = false>
 __device__ __forceinline__ void gc_split(float2 v, uint32_t& hi, uint32_t& lo) {
-    const float2 h = make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFFE000u),
-                                 __uint_as_float(__float_as_uint(v.y) & 0xFFFFE000u));
-    hi = gc_half2(h);
+    float2 h = make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFFE000u),
+                           __uint_as_float(__float_as_uint(v.y) & 0xFFFFE000u));
+    hi = gc_half2(ROUND ? v : h);
+    if (ROUND) h = __half22float2(*reinterpret_cast<__half2*>(&hi));
     lo = gc_half2(__ffma2_rn(h, make_float2(-1.0f, -1.0f), v));  // (an FMA: a packed sum has no sign)
 }
 
@@ -1011,7 +1016,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1)
                     if (c < n) {
                         uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int j = 0; j < 8; j++) gc_split(S[8 * e + j], hi[j], lo[j]);
+                        for (int j = 0; j < 8; j++) gc_split<true>(S[8 * e + j], hi[j], lo[j]);
                         if (e > 0) gc_stored(&sh.sfull[e - 1]);
                         gc_st8(tq + TC_SHI + 32 * hf + 8 * e, hi);
                         gc_st8(tq + TC_SLO + 32 * hf + 8 * e, lo);

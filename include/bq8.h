@@ -279,7 +279,9 @@ int gated_delta_decode(const bq_heads* q, const bq_heads* k, const bq_heads* v, 
  * cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device int32 [seqs + 1]; NULL: one sequence of all rows).  A
  * sequence may be empty (its state stays); bounds that are negative, past `total` or out of order make
  * the sequence empty.  Rows of no sequence keep their outputs.  Runs in chunks of 64 tokens on the
- * tensor cores, fp32-accurate (every fp32 operand as two scaled FP16 terms); a NaN or an infinity in a
+ * tensor cores.  The state is fp32-accurate (every fp32 operand of its products is two scaled FP16 terms); the
+ * products that only reach the BF16 outputs take one FP16 term of each operand, rounded to nearest: 2^-11 of
+ * every term beside the outputs' own rounding.  A NaN or an infinity in a
  * token reaches the outputs of its whole chunk, earlier tokens among them.  No stride of q, k or v
  * may be 0 (but for a dimension of one); head_dim must be 128; scratch:
  * bq_gated_delta_prefill_scratch_bytes(seqs, total, heads_k, heads_v) bytes, 16-byte aligned (about
