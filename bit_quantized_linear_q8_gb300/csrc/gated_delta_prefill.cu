@@ -79,6 +79,10 @@ constexpr int GC_C = 64;   // tokens a chunk
 constexpr int GC_D = 128;  // head dimension
 constexpr float GC_EPS = 1e-6f;
 constexpr int GC_MAX_SORT = 384;              // sequences that are ordered by length
+// Rows of the new state and of R are scaled as if their largest value were at least this times what stands for
+// 1 in the state before: a row that is all zeros beside a large state would otherwise get a scale whose product
+// with the state's own leaves fp32, and 0 times that is NaN.  Only rows 2^-115 below the state's bound see it.
+constexpr float GC_FLOOR = 0x1p-100f;
 
 // A chunk in the scratch.  Per key head the FP16 rows [K 64; Q 64] in two halves of the head
 // dimension (128-byte rows, 128-byte swizzle); per value head T hi, T lo and P (64 x 64 FP16, the same
@@ -986,11 +990,11 @@ __global__ void __launch_bounds__(GC_THREADS, 1)
                 float a = 1.0f, b = 0.0f;
                 if (c > 0) {
                     const float dec = scals[(c - 1) & 3].dec;
-                    most = fmaf(most, dec, sh.dmax[prev][0][dv] + sh.dmax[prev][1][dv]);
-                    a = dec;
+                    most = fmaxf(fmaf(most, dec, sh.dmax[prev][0][dv] + sh.dmax[prev][1][dv]), old * GC_FLOOR);
+                    a = dec * old;  // (before the new scale: dec may be zero and s * old above fp32)
                 }
                 float s = gc_pow2(most, inv);
-                a *= s * old;
+                a *= s;
                 b = dinv * s;
                 const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
                 if (hf == 0) sh.sinv[c & 3][dv] = inv;
@@ -1035,7 +1039,7 @@ __global__ void __launch_bounds__(GC_THREADS, 1)
                 // ---- R = beta v - (beta e^b rk) S^T k, scaled by a power of two from a bound on the row, so
                 // that all but one FMA and the split is done before S^T k is there
                 float rinv;
-                s = gc_pow2(fmaf(sc.crmax * inv, kbound, fmaxf(sh.vmax[prev][0][dv], sh.vmax[prev][1][dv])), rinv);
+                s = gc_pow2(fmaxf(fmaf(sc.crmax * inv, kbound, fmaxf(sh.vmax[prev][0][dv], sh.vmax[prev][1][dv])), inv * GC_FLOOR), rinv);
                 const float2 s2 = make_float2(s, s), cs2 = make_float2(-inv * s, -inv * s);
 #pragma unroll
                 for (int j = 0; j < 16; j++) bv[j] = __fmul2_rn(bv[j], s2);

@@ -1,9 +1,11 @@
-"""The gated delta rule at the ends of its range: queries that are stored keys."""
+"""The gated delta rule at the ends of its range: very large states, chunks that write nothing, queries
+that are stored keys.  Bounds as in test_gated_delta_gpu.py unless a test derives its own."""
 import numpy as np
 import pytest
 import torch
 
 from helpers import bf16_half_ulp
+from test_gated_delta_gpu import check, make, reference
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -16,6 +18,63 @@ def B():
     build.build()
     import bit_quantized_linear_q8_gb300 as B
     return B
+
+
+def both_forms(B, args, state, tokens, **kw):
+    """(name, out, new state) of the prefill and of single-token calls."""
+    s = state.clone()
+    yield "prefill", B.gated_delta_prefill(*args, s, **kw), s
+    s = state.clone()
+    out = [B.gated_delta_decode(*(a[t:t + 1] for a in args), s, **kw) for t in range(tokens)]
+    yield "decode", torch.cat(out), s
+
+
+@pytest.mark.parametrize("size", [1e5, 1e6, 1e20, 1e35])
+@pytest.mark.parametrize("tokens", [1, 64, 65, 130])
+def test_large_state_that_nothing_writes(B, size, tokens):
+    # beta = 0 everywhere: the state decays by e^(sum g) and nothing else happens
+    q, k, v, g, beta, state = make(tokens, tokens, 1, 2, 1, decay=0.01)
+    beta.zero_()
+    g[:, 0] = 0
+    state *= 10 * size
+    state[0, :, :, 5] = 0  # a column of zeros beside the large ones
+    ref = reference(q, k, v, g, beta, state, [tokens])
+    for what, out, s in both_forms(B, (q, k, v, g, beta), state, tokens):
+        assert torch.equal(s[0, 0], state[0, 0]), what
+        check(out, s, ref, what)
+
+
+@pytest.mark.parametrize("size", [1e5, 1e20, 1e35])
+@pytest.mark.parametrize("tokens", [1, 64, 65, 130])
+@pytest.mark.parametrize("forget", [float("-inf"), -500.0])
+def test_large_state_is_forgotten(B, size, tokens, forget):
+    # the first token forgets the state: the rest is as from a state of zeros, also where nothing is
+    # written (v = 0 in a few columns, beta = 0 in one head)
+    q, k, v, g, beta, state = make(tokens + 1, tokens, 1, 2, 1)
+    v = v.clone()
+    v[:, :, 3:9] = 0
+    beta[:, 1] = 0
+    g[0] = forget
+    state *= 10 * size
+    ref = reference(q, k, v, g, beta, torch.zeros_like(state), [tokens])
+    for what, out, s in both_forms(B, (q, k, v, g, beta), state, tokens):
+        check(out, s, ref, what)
+        assert not s[0, 1].any() and not s[0, 0, :, 3:9].any(), what
+
+
+def test_large_state_forgotten_in_mid_prompt(B):
+    # a chunk that writes nothing, then one that forgets, then ordinary ones; compared with a start from zeros there
+    q, k, v, g, beta, state = make(9, 300, 1, 2, 1)
+    state *= 1e21
+    beta[:64] = 0
+    g[:64] = 0
+    g[64] = float("-inf")
+    zero = torch.zeros_like(state)
+    rest = (q[64:], k[64:], v[64:], g[64:], beta[64:])
+    ref = reference(*rest, zero, [236])
+    for what, out, s in both_forms(B, (q, k, v, g, beta), state, 300):
+        check(out[64:], s, ref, what)
+        assert torch.isfinite(out[:64]).all(), what
 
 
 def test_queries_that_are_stored_keys(B):
