@@ -394,7 +394,8 @@ __device__ __forceinline__ bool gp_chunk(const CUtensorMap* mapQ, const CUtensor
         uint8_t* at = tile + pt * 128;
         const bool in = row < live_rows;
         const int x7 = row & 7;
-        float m;
+        float m = 0.0f;  // a bound on the row: its norm, or its largest magnitude
+        bool by_max = !p.l2norm;
         if (p.l2norm) {
             float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 4
@@ -411,7 +412,9 @@ __device__ __forceinline__ bool gp_chunk(const CUtensorMap* mapQ, const CUtensor
             const float ss = in ? a.x + a.y : 0.0f;
             rn = __fdiv_rn(1.0f, __fsqrt_rn(ss + GC_EPS));
             m = __fsqrt_rn(ss);
-        } else {
+            by_max = in && ss < 0x1p-100f;  // squares that underflow say nothing about the values
+        }
+        if (by_max) {
             uint32_t a = 0, b = 0;  // largest magnitudes of the even and odd values, as bit patterns
 #pragma unroll 4
             for (int x = 0; x < 16; x++) {
@@ -423,7 +426,8 @@ __device__ __forceinline__ bool gp_chunk(const CUtensorMap* mapQ, const CUtensor
                     b = max(b, (u[i] << 16) & 0x7FFF0000u);
                 }
             }
-            m = in ? __uint_as_float(max(a, b)) : 0.0f;
+            // (a norm of 128 values is below 12 times the largest)
+            m = in ? __uint_as_float(max(a, b)) * (p.l2norm ? 12.0f : 1.0f) : 0.0f;
         }
         const uint32_t e = max(__float_as_uint(m) >> 23, 8u);
         const float sc = __uint_as_float((261u - e) << 23);

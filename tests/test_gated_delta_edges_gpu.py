@@ -1,5 +1,6 @@
-"""The gated delta rule at the ends of its range: very large states, chunks that write nothing, queries
-that are stored keys.  Bounds as in test_gated_delta_gpu.py unless a test derives its own."""
+"""The gated delta rule at the ends of its range: very large states, chunks that write nothing, keys and
+queries that underflow, queries that are stored keys.  Bounds as in test_gated_delta_gpu.py unless a
+test derives its own."""
 import numpy as np
 import pytest
 import torch
@@ -75,6 +76,33 @@ def test_large_state_forgotten_in_mid_prompt(B):
     for what, out, s in both_forms(B, (q, k, v, g, beta), state, 300):
         check(out[64:], s, ref, what)
         assert torch.isfinite(out[:64]).all(), what
+
+
+@pytest.mark.parametrize("tokens", [1, 70])
+def test_normalised_rows_that_underflow(B, tokens):
+    # sums of squares that are subnormal or zero in fp32: x / sqrt(0 + 1e-6) is tiny, not NaN
+    q, k, v, g, beta, state = make(21, tokens, 2, 4, 1, normed=False)
+    sizes = torch.tensor([1e-18, 1e-20, 1e-22, 3e-24, 1e-25, 1e-28, 1e-33, 1e-37, 2e-39, 0.0])
+    for t in range(tokens):
+        k[t, t % 2] *= sizes[t % 10].item()
+        q[t, (t + 1) % 2] *= sizes[(t + 4) % 10].item()
+    ref = reference(q, k, v, g, beta, state, [tokens], l2norm=True)
+    for what, out, s in both_forms(B, (q, k, v, g, beta), state, tokens, l2norm=True):
+        check(out, s, ref, what)
+
+
+def test_one_tiny_row_keeps_its_digits(B):
+    # with a key of 1e-25 and no normalisation of the query, the output is that of the scaled key
+    q, k, v, g, beta, state = make(22, 1, 1, 1, 1, normed=False)
+    k *= 1e-25
+    q *= 1e-25
+    ref = reference(q, k, v, g, beta, state, [1], l2norm=True)
+    for what, out, s in both_forms(B, (q, k, v, g, beta), state, 1, l2norm=True):
+        o = ref[0].numpy()
+        # a query of 1e-22 after the norm: 2^-10 of sum |S q|, which random signs keep below 128 x the mean
+        lim = bf16_half_ulp(o) * (1 + 2.0 ** -7) + 2.0 ** -10 * (state.double().abs().amax() * q.double().abs().sum() * 1e3).item() * D ** -0.5
+        assert np.all(np.abs(out.cpu().double().numpy() - o) <= lim), what
+        assert np.abs(out.cpu().double().numpy()).max() > 0, what
 
 
 def test_queries_that_are_stored_keys(B):
