@@ -85,7 +85,8 @@ __device__ __forceinline__ int nq_round(float t) { return __float2int_rz(t + cop
 
 // Codes of one row from its scale.  y / s is y times RN(1/s), within 2 units in the last place of
 // the quotient, so a code can differ from the exact quotient's only where that lies as close to
-// a half-way point.  Scales whose reciprocal is not a normal number take the division.  A row
+// a half-way point.  Scales whose reciprocal is not a normal number take the division, and as a subnormal
+// scale is rounded to whole units of 2^-149 (128 to 190 units of |y| to one), their codes stop at 127.  A row
 // with a NaN or an infinity has the scale NaN or infinity (its decoded values are NaN) and codes 0.
 struct NqScale {
     float s, inv;
@@ -96,9 +97,10 @@ struct NqScale {
         divide = amax < 1e-30f;
         inv = none || divide ? 0.0f : __frcp_rn(s);
     }
+    __device__ __forceinline__ int divided(float y) const { return min(max(nq_round(__fdiv_rn(y, s)), -127), 127); }
     __device__ __forceinline__ int code(float y) const {
         if (none) return 0;
-        return nq_round(divide ? __fdiv_rn(y, s) : y * inv);
+        return divide ? divided(y) : nq_round(y * inv);
     }
     // Eight codes; whether to divide is decided once (a division beside every product took the
     // kernel twice as long).  Without codes inv is 0, and 0 times anything rounds to the code 0.
@@ -106,8 +108,8 @@ struct NqScale {
         if (divide && !none) {
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                q[2 * j] = nq_round(__fdiv_rn(y[j].x, s));
-                q[2 * j + 1] = nq_round(__fdiv_rn(y[j].y, s));
+                q[2 * j] = divided(y[j].x);
+                q[2 * j + 1] = divided(y[j].y);
             }
         } else {
 #pragma unroll
