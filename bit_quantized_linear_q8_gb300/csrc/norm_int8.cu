@@ -67,6 +67,13 @@ __device__ __forceinline__ float nq_max_abs(float m, float v) {
     return r;
 }
 
+// 1 / sqrt(mean(h^2) + eps) from the sum of squares.  A sum that leaves fp32 (finite values above 2^63 or so) would
+// give 0 and a row of zeros without a sign of it: NaN, so that the row reads as NaN.
+__device__ __forceinline__ float nq_inv_rms(float ss, const NqArgs& p) {
+    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.k) + p.eps));
+    return ss <= 3.4028235e38f ? rs : __int_as_float(0x7fffffff);
+}
+
 // The arithmetic runs on pairs (packed fp32: two values an instruction, each rounded as alone).
 __device__ __forceinline__ void nq_unpack8(const uint4& w, float2 (&v)[4]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -173,7 +180,7 @@ __global__ void __launch_bounds__(1024) norm_int8_kernel(const NqArgs p, int T) 
     float amax = 0.0f;
     if (NORM) {
         const float ss = nq_reduce<false>(s2.x + s2.y, red[0], nw);
-        const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.k) + p.eps));
+        const float rs = nq_inv_rms(ss, p);
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const int c = t + i * T;
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(1024) norm_int8_any_kernel(const NqArgs p) {
             ss = fmaf(h, h, ss);
         }
         ss = nq_reduce<false>(ss, red[0], nw);
-        rs = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.k) + p.eps));
+        rs = nq_inv_rms(ss, p);
     }
     auto y_at = [&](uint32_t c) { return NORM ? h_at(c) * rs * bf16_bits_to_f32(p.weight[c]) : h_at(c); };
     float amax = 0.0f;

@@ -206,8 +206,8 @@ int dequant_nvfp4_to_bf16(const void* packed, const void* scales, uint16_t* out,
  * int8 with one scale a row: codes [rows][k] int8, scales [rows] fp32, value = code * scale.
  * A row is a token of activations or an output channel of a weight.  s = max|y| / 127, code =
  * round-half-away(y / s) in fp32, 0 for a row of zeros.  A row that holds a NaN or an infinity
- * (or whose sum of squares leaves the fp32 range) gets a NaN or infinite scale and codes 0: its
- * values read as NaN. */
+ * (or, in the norms, whose sum of squares leaves the fp32 range) gets a NaN or infinite scale and codes 0: its
+ * values read as NaN, and those of a norm's y_out are NaN. */
 
 /* Residual addition, root-mean-square norm and int8 codes in one pass over [m][k]:
  *   h = x + residual (fp32);  y = h / sqrt(mean(h^2) + eps) * weight (fp32, not rounded);
