@@ -470,7 +470,7 @@ template <int T>
 static int launch_t(const uint8_t* codes, const CUtensorMap& xmap, const uint16_t* scales, uint16_t* y, int m,
                     int n, int k, int group, int ntiles, int ncta, int ksplit, uint16_t* hgate, cudaStream_t stream,
                     const char* who) {
-    static int configured_smem[64] = {0};
+    static int configured[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64) dev = 63;
@@ -483,11 +483,12 @@ static int launch_t(const uint8_t* codes, const CUtensorMap& xmap, const uint16_
     while (nstages > 2 && fixed + nstages * stage > (size_t)GEMV_SMEM_SHARE) nstages--;
     const size_t smem = fixed + nstages * stage;
     if (smem > (size_t)GEMV_SMEM_LIMIT) return fail(BQ_ERR_INVALID, "%s: shape needs too much shared memory", who);
-    if ((size_t)configured_smem[dev] < smem) {
-        if (cudaFuncSetAttribute(q2_gemv_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+    // (the most that any shape takes, so that threads with different shapes all write the same limit)
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(q2_gemv_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMV_SMEM_LIMIT) !=
             cudaSuccess)
-            return fail(BQ_ERR_LAUNCH, "%s: cannot reserve %zu bytes of shared memory", who, smem);
-        configured_smem[dev] = (int)smem;
+            return fail(BQ_ERR_LAUNCH, "%s: cannot reserve %d bytes of shared memory", who, GEMV_SMEM_LIMIT);
+        configured[dev] = 1;
     }
     // codes boxes of exactly T and T-1 tiles of rows (CTAs get one or the other)
     CUtensorMap map_full, map_less;

@@ -743,7 +743,7 @@ static HmKernel hm_kernel_for(uint32_t m) {
 // y2 gets u).
 static int launch_hm(const uint16_t* x, const bq_q2_weight* w, const bq_q2_weight* w2, uint16_t* y, uint16_t* y2,
                      uint32_t m, uint16_t* hgate, cudaStream_t stream, const char* who) {
-    static int configured_smem[64][5][8] = {};
+    static int configured[64][5][8] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64) dev = 63;
@@ -762,10 +762,11 @@ static int launch_hm(const uint16_t* x, const bq_q2_weight* w, const bq_q2_weigh
     const HmKernel kern = prm.hpc == 4 ? hm_kernel_for<false, true, 4>(m)
                           : dual ? (unr ? hm_kernel_for<true, true, 2>(m) : hm_kernel_for<true, false, 2>(m))
                                  : (unr ? hm_kernel_for<false, true, 2>(m) : hm_kernel_for<false, false, 2>(m));
-    if ((size_t)configured_smem[dev][kind][m - 1] < smem) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-            return fail(BQ_ERR_LAUNCH, "%s: cannot reserve %zu bytes of shared memory", who, smem);
-        configured_smem[dev][kind][m - 1] = (int)smem;
+    // (the most that any shape takes, so that threads with different shapes all write the same limit)
+    if (!configured[dev][kind][m - 1]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, HM_SMEM_LIMIT) != cudaSuccess)
+            return fail(BQ_ERR_LAUNCH, "%s: cannot reserve %d bytes of shared memory", who, HM_SMEM_LIMIT);
+        configured[dev][kind][m - 1] = 1;
     }
     // rows of a whole number of 128-byte column blocks (k % 512 == 0): one 3-D request brings a chunk's
     // column blocks; otherwise one 2-D box per 512-column half

@@ -772,15 +772,16 @@ static IgPlan ig_plan(uint32_t m, uint32_t n, uint32_t k) {
 template <bool PRE>
 static int ig_launch(const CUtensorMap& mw, const CUtensorMap& mx, const int8_t* xc, const float* sa, const float* sw, uint16_t* out,
                      uint32_t m, uint32_t n, uint32_t k, const IgPlan& pl, cudaStream_t stream, const char* who) {
-    static uint32_t configured[64] = {};
+    // the most that any plan takes, so that threads with different plans all write the same limit
+    static int configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) dev = 63;
-    if (configured[dev] < pl.smem) {
-        if (cudaFuncSetAttribute(int8_gemm_kernel<PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem) !=
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(int8_gemm_kernel<PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)IG_SMEM1) !=
             cudaSuccess)
-            return fail(BQ_ERR_LAUNCH, "%s: cannot reserve %u bytes of shared memory", who, pl.smem);
-        configured[dev] = pl.smem;
+            return fail(BQ_ERR_LAUNCH, "%s: cannot reserve %u bytes of shared memory", who, IG_SMEM1);
+        configured[dev] = 1;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pl.grid);
