@@ -205,28 +205,33 @@ __device__ __forceinline__ bool mbar_wait_suspend(uint64_t* bar, uint32_t parity
 // The wait of the kernels whose steps are a few hundred cycles: the loop is kept in one piece, so a
 // phase that is already complete costs one try_wait and one branch (the C loops above cost two to
 // three times that in long kernels).  Gives up (false) after 2^22 tries, about a tenth of a second.
-// Every lane of a converged warp gets the same answer.
+// Every lane of a converged warp gets the same answer.  CLUSTER: for a barrier with arrivals from other CTAs.
+#define BQ8_WAIT_LEAN(SCOPE)                                               \
+    asm volatile(                                                          \
+        "{\n"                                                              \
+        ".reg .pred p, q;\n"                                               \
+        ".reg .u32 c;\n"                                                   \
+        "mov.u32 c, 4194304;\n"                                            \
+        "WAIT:\n"                                                          \
+        "mbarrier.try_wait.parity" SCOPE ".shared::cta.b64 p, [%1], %2;\n" \
+        "@p bra DONE;\n"                                                   \
+        "sub.u32 c, c, 1;\n"                                               \
+        "setp.ne.u32 q, c, 0;\n"                                           \
+        "@q bra WAIT;\n"                                                   \
+        "DONE:\n"                                                          \
+        "selp.u32 %0, 1, 0, p;\n"                                          \
+        "}\n"                                                              \
+        : "=r"(done)                                                       \
+        : "r"(smem_u32(bar)), "r"(parity)                                  \
+        : "memory")
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_lean(uint64_t* bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n"
-        ".reg .pred p, q;\n"
-        ".reg .u32 c;\n"
-        "mov.u32 c, 4194304;\n"
-        "WAIT:\n"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "@p bra DONE;\n"
-        "sub.u32 c, c, 1;\n"
-        "setp.ne.u32 q, c, 0;\n"
-        "@q bra WAIT;\n"
-        "DONE:\n"
-        "selp.u32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if (CLUSTER) BQ8_WAIT_LEAN(".relaxed.cluster");
+    else BQ8_WAIT_LEAN("");
     return done != 0;
 }
+#undef BQ8_WAIT_LEAN
 
 // (a & b) | c in one LOP3 with all three operands in registers.
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {

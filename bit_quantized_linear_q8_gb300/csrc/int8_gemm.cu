@@ -9,7 +9,7 @@
 //    to 128 weight rows (output channels = tensor-memory lanes) x N tokens (columns).  Expanding
 //    the codes into tensor memory instead of shared memory keeps the expanded weight out of
 //    the shared-memory port, which the activations' reads already fill.  An M128 N K16 MMA takes
-//    about 34 + N / 2 cycles this way, 32 more with A in shared memory.
+//    about 34 + N / 2 cycles in these steps, 32 more with A in shared memory (alone and back to back N / 2).
 //  * Weight codes stream through a ring of TMA boxes, R rows of 128 bytes (16 KB, 128-byte
 //    swizzle).  Warps 4-11 (two groups of four, one lane quadrant a warp, one weight row a
 //    thread; the groups take alternate steps) expand them: a byte permute puts code + 128 into
@@ -25,8 +25,11 @@
 //    memory.  Warps 4-11 read the accumulator, scale and store.
 //  * Large-m form: a kernel expands the codes once into the caller's scratch (2 m k bytes) and
 //    warp 2 streams FP16 boxes by TMA.  Pairs of CTAs of a cluster run neighbouring weight tiles of
-//    the same tokens, and each fetches half of every token box for both.  Warps 12-19 store, so
-//    that the expanding warps go on with the next tile.
+//    the same tokens as one M 256 MMA (cta_group::2): the weight rows in each CTA's own tensor memory, half of
+//    every token box in each CTA's shared memory.  The first CTA issues for both; the second's expanding and
+//    storing warps arrive on its barriers, relaxed (tensor memory is ordered by the tcgen05 fences; with a
+//    release, which waits for the thread's other accesses, 2048 x 16384 x 5120 took 233 us, 188 without).
+//    Warps 12-19 store, so that the expanding warps go on with the next tile.
 //  * Few tiles: the K steps of a tile are split over a cluster of up to 8 CTAs, whose fp32
 //    partial sums meet through distributed shared memory in a fixed order (ig_plan).
 //  * Launched programmatically: the setup runs while the kernel before drains (every launch 2 us
@@ -37,7 +40,8 @@
 // Bound: small m by the weight's bytes, n k at the memory's rate, beside a fixed 6 us of launch,
 // ring filling and reduction (16384 x 5120: 19.5 us at m = 1; 16384 x 20480: 62 us, 6.4 TB/s
 // beyond the fixed part); large m by the tensor cores, with the expansion beside it (m = 2048,
-// 16384 x 5120: 189 us, 1.82 PFLOP/s, the expansion of the activations included).
+// 16384 x 5120: 188 us, 1.83 PFLOP/s, in a run of a few milliseconds, 200 us under the power cap of a long one,
+// the expansion of the activations included).
 #include "common.cuh"
 
 namespace bq8 {
@@ -84,22 +88,23 @@ __device__ __forceinline__ uint32_t ig_elect() {
     return r;
 }
 
-// Arrival on `bar` once the MMAs issued before are done; with `pair` on the barriers at the same place
-// in both CTAs of a pair.
-__device__ __forceinline__ void ig_commit(uint64_t* bar, uint32_t one) {
-    asm volatile(
-        "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
-        "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void ig_commit_pair(uint64_t* bar, uint32_t mask, uint32_t one) {
-    asm volatile(
-        "{\n.reg .pred e;\nsetp.ne.u32 e, %2, 0;\n"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)mask), "r"(one)
-        : "memory");
+// Arrival on `bar` once the MMAs issued before are done; in a pair on the barriers at the same place in both
+// of its CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void ig_commit(uint64_t* bar, uint32_t both, uint32_t one) {
+    if (PAIR)
+        asm volatile(
+            "{\n.reg .pred e;\nsetp.ne.u32 e, %2, 0;\n"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)both), "r"(one)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+            "r"(one)
+            : "memory");
 }
 
 // Arrival of a warp, by one lane and without a branch.
@@ -110,12 +115,22 @@ __device__ __forceinline__ void ig_arrive(uint64_t* bar, uint32_t one) {
         : "memory");
 }
 
-// A tile load into the same place of both CTAs of a pair, its bytes counted on both barriers.
-__device__ __forceinline__ void ig_tma_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint32_t mask) {
+// The same on a barrier of another CTA of the cluster (an address of ig_cluster_addr), after tcgen05 operations that
+// were waited for and fenced: tensor memory needs no release of the thread's other accesses, which waits
+// for all of them.
+__device__ __forceinline__ void ig_arrive_cluster(uint32_t addr, uint32_t one) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
-        "{%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"((uint16_t)mask)
+        "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n@e mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}\n" ::"r"(addr),
+        "r"(one)
+        : "memory");
+}
+
+// A tile load into this CTA whose bytes are counted on a barrier of the pair's first CTA.
+__device__ __forceinline__ void ig_tma_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 
@@ -129,13 +144,21 @@ __device__ __forceinline__ uint64_t ig_desc(uint32_t addr) {
            (2ull << 61);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, FP16 in, fp32 accumulate, K 16, by the lane with `one`.
+// D[tmem] (+)= A[tmem] * B[smem]^T, FP16 in, fp32 accumulate, K 16, by the lane with `one`; for a pair M 256,
+// the lanes of either CTA's tensor memory against the rows of B in both CTAs' shared memory.
+template <bool PAIR>
 __device__ __forceinline__ void ig_mma(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
                                        uint32_t one) {
-    asm volatile(
-        "{\n.reg .pred p, e;\nsetp.ne.u32 p, %3, 0;\nsetp.ne.u32 e, %5, 0;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(accumulate), "r"(idesc), "r"(one));
+    if (PAIR)
+        asm volatile(
+            "{\n.reg .pred p, e;\nsetp.ne.u32 p, %3, 0;\nsetp.ne.u32 e, %5, 0;\n"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %4, p;\n}\n" ::"r"(d),
+            "r"(a), "l"(bdesc), "r"(accumulate), "r"(idesc), "r"(one));
+    else
+        asm volatile(
+            "{\n.reg .pred p, e;\nsetp.ne.u32 p, %3, 0;\nsetp.ne.u32 e, %5, 0;\n"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n}\n" ::"r"(d),
+            "r"(a), "l"(bdesc), "r"(accumulate), "r"(idesc), "r"(one));
 }
 
 __device__ __forceinline__ void ig_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -205,8 +228,9 @@ __device__ __forceinline__ void ig_store(uint16_t* __restrict__ out, size_t at, 
     out[at] = *reinterpret_cast<const uint16_t*>(&b);
 }
 
-// PRE: the activations come expanded (FP16 [m][k]); otherwise as codes.
-template <bool PRE>
+// PRE: the activations come expanded (FP16 [m][k]); otherwise as codes.  PAIR (of PRE): two CTAs run two
+// neighbouring weight tiles of the same tokens as one M 256 MMA.
+template <bool PRE, bool PAIR>
 __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
                      const int8_t* __restrict__ xc, const float* __restrict__ sa, const float* __restrict__ sw,
@@ -214,7 +238,7 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
     extern __shared__ uint8_t smem_raw[];
     uint8_t* aring = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (stays a shared address for the compiler)
     constexpr int COLS = PRE ? 512 : 256;           // tensor-memory columns
-    const uint32_t xbytes = (uint32_t)pl.N * 128u;  // a 128-byte row per token
+    const uint32_t xbytes = (uint32_t)pl.N * (PAIR ? 64u : 128u);  // a 128-byte row per token (of half of a pair's)
     uint8_t* xring = aring + pl.nA * IG_ASTAGE;     // activation codes (not PRE)
     uint8_t* bring = xring + (PRE ? 0 : 2 * pl.xd * xbytes);
     uint64_t* afull = reinterpret_cast<uint64_t*>(bring + pl.nB * xbytes);
@@ -230,10 +254,13 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
     int* failed = reinterpret_cast<int*>(tslot + 1);
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
-    const int split = pl.split, pair = PRE ? pl.pair : 1;
+    const int split = pl.split;
+    constexpr int pair = PAIR ? 2 : 1;
     // a cluster: `split` shares of K, in each of which `pair` CTAs run neighbouring weight tiles
     const int place = (int)(blockIdx.x % (uint32_t)(split * pair)), rank = place / pair, prank = place % pair;
     const uint32_t both = 3u << (place - prank);  // this CTA and its partner
+    // the pair's first CTA issues the MMAs; what they wait for arrives on its barriers
+    auto first_cta = [&](uint64_t* bar) { return ig_cluster_addr(smem_u32(bar), (uint32_t)(place - prank)); };
     const int SA = (k + 127) >> 7;  // K steps of 128 codes
     const int s0 = (int)((int64_t)SA * rank / split), s1 = (int)((int64_t)SA * (rank + 1) / split);
     const int first = blockIdx.x / (split * pair), stride = gridDim.x / (split * pair);
@@ -256,22 +283,26 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
         for (int s = 0; s < pl.nA; s++) mbar_init(&aempty[s], 4);  // one arrival per expanding warp
         for (int s = 0; s < pl.nB; s++) {
             mbar_init(&bfull[s], PRE ? 1u : (uint32_t)pl.halves);
-            mbar_init(&bempty[s], (uint32_t)pair);  // every CTA of a pair has read its copy
+            mbar_init(&bempty[s], 1);
         }
         for (int s = 0; s < pl.nT; s++) {
-            mbar_init(&tfull[s], 4);
+            mbar_init(&tfull[s], 4 * pair);
             mbar_init(&tempty[s], 1);
         }
         mbar_init(accf, 1);
-        mbar_init(acce, 8);
+        mbar_init(acce, 8 * pair);
         mbar_init(done, 1);
         *failed = 0;
         fence_barrier_init();
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)),
-                     "n"(COLS));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(COLS));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(COLS));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
         // The next kernel's CTAs may take free SM space from here on: not before the kernels before have
         // ended (some read their weights before they wait), nor before this CTA has its tensor
         // memory, which they could hold while they wait for this grid's end.
@@ -281,7 +312,7 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
     pdl_wait();  // the kernels before have ended: from here on memory is read and written
     ig_fence_before();
     __syncthreads();
-    if (pair > 1) ig_cluster_sync();  // both CTAs' barriers exist before any remote arrival
+    if (PAIR) ig_cluster_sync();  // both CTAs' barriers exist before any remote arrival
     ig_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
     const uint32_t tA = tbase + (uint32_t)(COLS - 64 * pl.nT);  // the A operand's stages
@@ -310,21 +341,23 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
                 if (!mbar_wait_suspend(&afull[j % pl.nA], (uint32_t)(j / pl.nA) & 1u)) atomicOr(&g_int8_gemm_status, 2u);
         }
         __syncwarp();
+    } else if (warp == 0 && prank > 0) {
+        // (the pair's first CTA issues for both)
     } else if (warp == 0) {
         // ---------------------------------------------------------------- MMA issuer
         // The whole warp runs the loop, so that every operand is warp-uniform, and one elected lane
         // issues (operands that the compiler cannot prove uniform cost 155 cycles an MMA).
         // D fp32 (bit 4), A and B FP16, both K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28
-        const uint32_t idesc = (1u << 4) | ((uint32_t)(pl.N >> 3) << 17) | ((uint32_t)(IG_BM >> 4) << 24);
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(pl.N >> 3) << 17) | ((uint32_t)(IG_BM * pair >> 4) << 24);
         const uint32_t bbase = __shfl_sync(0xffffffffu, smem_u32(bring), 0);
         const uint32_t one = ig_elect();
         IgPos t, b;
         bool ok = true;
         int ti = 0;
         for (int id = first; id < pl.ntiles && ok; id += stride, ti++) {
-            if (ti > 0) ok = mbar_wait_lean(acce, (uint32_t)(ti - 1) & 1u);
+            if (ti > 0) ok = mbar_wait_lean<PAIR>(acce, (uint32_t)(ti - 1) & 1u);
             for (int s = s0; s < s1 && ok; s++) {
-                ok = mbar_wait_lean(&tfull[t.s], t.p);
+                ok = mbar_wait_lean<PAIR>(&tfull[t.s], t.p);
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     ok &= mbar_wait_lean(&bfull[b.s], b.p);
@@ -333,17 +366,16 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
                     const uint32_t aa = tA + 64u * t.s + 32u * h;
 #pragma unroll
                     for (int kk = 0; kk < 4; kk++)
-                        ig_mma(tbase, aa + 8u * kk, bd + 2u * kk, idesc, h | kk ? 1u : (uint32_t)(s - s0), one);
-                    if (PRE && pair > 1) ig_commit_pair(&bempty[b.s], both, one);
-                    else ig_commit(&bempty[b.s], one);
+                        ig_mma<PAIR>(tbase, aa + 8u * kk, bd + 2u * kk, idesc, h | kk ? 1u : (uint32_t)(s - s0), one);
+                    ig_commit<PAIR>(&bempty[b.s], both, one);
                     b.next(pl.nB);
                 }
-                ig_commit(&tempty[t.s], one);
+                ig_commit<PAIR>(&tempty[t.s], both, one);
                 t.next(pl.nT);
             }
-            ig_commit(accf, one);
+            ig_commit<PAIR>(accf, both, one);
         }
-        ig_commit(done, one);  // completes once every MMA issued above has finished
+        ig_commit<PAIR>(done, both, one);  // completes once every MMA issued above has finished
         if (!mbar_wait_suspend(done, 0)) ok = false;
         if (!ok) *failed = 1;
     } else if (warp < 4 || (!PRE && warp >= 12)) {
@@ -360,16 +392,16 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
                             ok = false;
                             break;
                         }
-                        mbar_arrive_expect_tx(&bfull[b.s], xbytes);
-                        if (pair > 1)  // half of the tokens from either CTA, to both
-                            ig_tma_pair(bring + b.s * xbytes + prank * (xbytes / 2), &mapX, s * 128, m0 + prank * (pl.N / 2), &bfull[b.s],
-                                        both);
+                        if (prank == 0) mbar_arrive_expect_tx(&bfull[b.s], xbytes * pair);
+                        if (PAIR)  // half of the tokens in either CTA
+                            ig_tma_pair(bring + b.s * xbytes, &mapX, s * 128, m0 + prank * (pl.N / 2), first_cta(&bfull[b.s]));
                         else
                             tma_load_2d(bring + b.s * xbytes, &mapX, s * 128, m0, &bfull[b.s]);
                     }
                 }
                 if (!ok) *failed = 1;
-                for (int64_t j = cnt > pl.nB ? cnt - pl.nB : 0; j < cnt; j++)
+                // (a pair's first CTA waits for both; neither leaves before that)
+                for (int64_t j = cnt > pl.nB ? cnt - pl.nB : 0; j < cnt && prank == 0; j++)
                     if (!mbar_wait_suspend(&bfull[j % pl.nB], (uint32_t)(j / pl.nB) & 1u))
                         atomicOr(&g_int8_gemm_status, 2u);
             }
@@ -458,7 +490,7 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
         // ---------------------------------------------------------------- A operand (and epilogue)
         const int qd = warp & 3, g = (warp - 4) >> 2;
         const int row = 32 * qd + lane;
-        const uint32_t tq = (uint32_t)(32 * qd) << 16, one = lane == 0;
+        const uint32_t tq = (uint32_t)(32 * qd) << 16, one = lane == 0, tfull0 = PAIR ? first_cta(tfull) : 0u;
         IgPos a, t;
         int cnt = 0, ti = 0;
         bool ok = true;
@@ -488,7 +520,8 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 ig_fence_before();
                 __syncwarp();
-                ig_arrive(&tfull[t.s], one);
+                if (PAIR) ig_arrive_cluster(tfull0 + 8u * t.s, one);
+                else ig_arrive(&tfull[t.s], one);
                 ig_arrive(&aempty[a.s], one);
             }
             if (!PRE && ok) {
@@ -529,6 +562,7 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
         const int row = 32 * qd + lane;
         const uint32_t tq = (uint32_t)(32 * qd) << 16;
         const int half = pl.N / 2, odd = lane & 1;  // N is a multiple of 32 here
+        const uint32_t acce0 = PAIR ? first_cta(acce) : 0u;
         int ti = 0;
         for (int id = first; id < pl.ntiles; id += stride, ti++) {
             if (!mbar_wait_lean(accf, (uint32_t)ti & 1u)) {
@@ -564,7 +598,8 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
                 }
                 ig_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(acce);
+                if (PAIR) ig_arrive_cluster(acce0, lane == 0);
+                else ig_arrive(acce, lane == 0);
                 // Even n and R: neighbouring lanes exchange, the even one stores the pair's rows of the even
                 // tokens and the odd one those of the odd tokens.
                 const bool pairs = ((n | pl.R) & 1) == 0;
@@ -588,18 +623,25 @@ __global__ void __launch_bounds__(PRE ? IG_THREADS_PRE : IG_THREADS, PRE ? 1 : 2
             }
             ig_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acce);
+            if (PAIR) ig_arrive_cluster(acce0, lane == 0);
+            else ig_arrive(acce, lane == 0);
         }
     }
 
     ig_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *failed) atomicOr(&g_int8_gemm_status, 1u);
+    if (PAIR) {
+        // no MMA, copy or arrival of the pair is under way past this point
+        if (threadIdx.x == 0 && prank > 0 && !mbar_wait_suspend(done, 0)) atomicOr(&g_int8_gemm_status, 2u);
+        __syncwarp();
+        ig_cluster_sync();
+    }
     if (warp == 0) {
         ig_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "n"(COLS));
+        if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "n"(COLS));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "n"(COLS));
     }
-    if (pair > 1) ig_cluster_sync();  // no CTA leaves while the other may still copy into it
     if (split > 1) {
         // every CTA of the cluster sums the partials of its share of the tokens, rank by rank
         ig_cluster_sync();
@@ -690,9 +732,9 @@ static int ig_capacity(int size, int per_sm) {
 // SM takes from L2 (64 bytes a cycle); the CTAs of an SM add up.  A launch is as long as its fullest
 // SM's, plus what a tile costs beside its steps (filling the rings, the epilogue, the cluster's
 // reduction).  Tried: equal cuts of the tokens (up to 8 more than needed: 1000 x 5120 x 5120 in seven cuts
-// 55.6 us, 62.1 in four; 4096 x 5120 x 6144 164 us, 174 with 256 tokens a tile), weight rows a tile from
+// 51.7 us, 62 in four; 4096 x 5120 x 6144 152 us), weight rows a tile from
 // 128 down (tiles that divide more evenly among the SMs), clusters of up to 8 over K, and in the
-// large-m form over K and pairs of weight tiles (150 x 5120 x 17408: 37 us, 63 over K alone).
+// large-m form over K and pairs of weight tiles (150 x 5120 x 17408: 34.7 us, 63 over K alone).
 static IgPlan ig_plan(uint32_t m, uint32_t n, uint32_t k) {
     const bool pre = m > IG_SMALL_M;
     const int SA = (int)((k + 127) / 128), sms = sm_count();
@@ -710,7 +752,7 @@ static IgPlan ig_plan(uint32_t m, uint32_t n, uint32_t k) {
             if ((int64_t)p.ntm * (wt + 1) * 8 >= (1ll << 31)) continue;
             for (int cluster = 1; cluster <= 16; cluster++) {
                 // shares of K alone, then with pairs of weight tiles (which halve what an SM takes of the
-                // activations); one share always with pairs in the large-m form
+                // activations); the large-m form with more than one weight tile always has pairs where one share is taken
                 const int pair = cluster > 8 ? 2 : 1, split = cluster > 8 ? cluster - 8 : cluster;
                 if (split * pair > 8 || (split > 1 && SA < 2 * split)) continue;
                 if (pre && wt > 1 ? split == 1 && pair == 1 : pair == 2) continue;
@@ -741,7 +783,7 @@ static IgPlan ig_plan(uint32_t m, uint32_t n, uint32_t k) {
     }
     if (best.grid == 0) return best;
     IgPlan& p = best;
-    const uint32_t xbytes = (uint32_t)p.N * 128u;
+    const uint32_t xbytes = (uint32_t)p.N * 128u / p.pair;
     // two CTAs an SM (half of the shared memory and of tensor memory each) only where one an SM is
     // too few: the bytes in flight count, not the CTAs
     const int per_sm =
@@ -769,7 +811,7 @@ static IgPlan ig_plan(uint32_t m, uint32_t n, uint32_t k) {
     return best;
 }
 
-template <bool PRE>
+template <bool PRE, bool PAIR>
 static int ig_launch(const CUtensorMap& mw, const CUtensorMap& mx, const int8_t* xc, const float* sa, const float* sw, uint16_t* out,
                      uint32_t m, uint32_t n, uint32_t k, const IgPlan& pl, cudaStream_t stream, const char* who) {
     // the most that any plan takes, so that threads with different plans all write the same limit
@@ -778,7 +820,7 @@ static int ig_launch(const CUtensorMap& mw, const CUtensorMap& mx, const int8_t*
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) dev = 63;
     if (!configured[dev]) {
-        if (cudaFuncSetAttribute(int8_gemm_kernel<PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)IG_SMEM1) !=
+        if (cudaFuncSetAttribute(int8_gemm_kernel<PRE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)IG_SMEM1) !=
             cudaSuccess)
             return fail(BQ_ERR_LAUNCH, "%s: cannot reserve %u bytes of shared memory", who, IG_SMEM1);
         configured[dev] = 1;
@@ -797,7 +839,7 @@ static int ig_launch(const CUtensorMap& mw, const CUtensorMap& mx, const int8_t*
     cfg.attrs = at;
     cfg.numAttrs = pl.split * pl.pair > 1 ? 2 : 1;
     const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, int8_gemm_kernel<PRE>, mw, mx, xc, sa, sw, out, (int)m, (int)n, (int)k, pl);
+        cudaLaunchKernelEx(&cfg, int8_gemm_kernel<PRE, PAIR>, mw, mx, xc, sa, sw, out, (int)m, (int)n, (int)k, pl);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(e == cudaErrorNoKernelImageForDevice ? BQ_ERR_UNSUPPORTED : BQ_ERR_LAUNCH, "%s: launch failed: %s", who,
@@ -846,7 +888,7 @@ extern "C" int int8_gemm(const int8_t* a, const float* sa, const int8_t* w, cons
     CUtensorMap mw, mx;
     int st = cached_tmap_2d_u8(&mw, w, k, n, k, 128, (uint32_t)pl.R, true, who);
     if (st) return st;
-    if (!need) return ig_launch<false>(mw, mw, a, sa, sw, out, m, n, k, pl, (cudaStream_t)stream, who);
+    if (!need) return ig_launch<false, false>(mw, mw, a, sa, sw, out, m, n, k, pl, (cudaStream_t)stream, who);
     if ((st = cached_tmap_2d_u8(&mx, scratch, (uint64_t)k * 2, m, (uint64_t)k * 2, 128, (uint32_t)(pl.N / pl.pair), true,
                                 who)))
         return st;
@@ -855,5 +897,6 @@ extern "C" int int8_gemm(const int8_t* a, const float* sa, const int8_t* w, cons
     if ((st = launch_programmatic(who, int8_expand_kernel, (uint32_t)(want < most ? want : most), 256, 0, (cudaStream_t)stream,
                                   reinterpret_cast<const uint4*>(a), reinterpret_cast<uint4*>(scratch), total)))
         return st;
-    return ig_launch<true>(mw, mx, nullptr, sa, sw, out, m, n, k, pl, (cudaStream_t)stream, who);
+    return pl.pair > 1 ? ig_launch<true, true>(mw, mx, nullptr, sa, sw, out, m, n, k, pl, (cudaStream_t)stream, who)
+                       : ig_launch<true, false>(mw, mx, nullptr, sa, sw, out, m, n, k, pl, (cudaStream_t)stream, who);
 }
