@@ -78,9 +78,11 @@ def _need(t, dtype, name, shape=None):
     return t
 
 
-def _need_bytes(t, nbytes, name):
-    """A uint8 CUDA buffer of at least `nbytes` bytes."""
+def _need_bytes(t, nbytes, name, device=None):
+    """A uint8 CUDA buffer of at least `nbytes` bytes, on `device` where one is given."""
     _need(t, _torch().uint8, name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the call's tensors on %s" % (name, t.device, device))
     if t.numel() < nbytes:
         raise ValueError("%s holds %d bytes, needs %d" % (name, t.numel(), nbytes))
     return t
@@ -424,7 +426,7 @@ def int8_gemm(a, a_scales, w, w_scales, out=None, scratch=None):
         if scratch is None:
             scratch = torch.empty(need, dtype=torch.uint8, device=a.device)
         else:
-            _need_bytes(scratch, need, "scratch")
+            _need_bytes(scratch, need, "scratch", a.device)
     check(lib().int8_gemm(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(out), _ptr(scratch) if need else None,
                           m, n, k, _stream()))
     return out
@@ -520,7 +522,7 @@ def gated_delta_prefill(q, k, v, g, beta, state, cu_seqlens=None, state_idx=None
     if scratch is None:
         scratch = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
-        _need_bytes(scratch, need, "scratch")
+        _need_bytes(scratch, need, "scratch", q.device)
     b = ctypes.byref
     check(lib().gated_delta_prefill(b(d[0]), b(d[1]), b(d[2]), b(d[3]), b(d[4]), _ptr(state), _ptr(cu_seqlens),
                                     _ptr(state_idx), _ptr(out), _ptr(scratch), seqs, total, hk, hv, dim, state.shape[0],
