@@ -106,7 +106,8 @@ constexpr uint32_t GC_TP = 3 * GC_TILE + 2048;  // stride
 static_assert(GC_TP_BYTES <= GC_TP && GC_TP_BYTES % 16 == 0, "scratch block");
 
 // Chunk c of sequence s has the slot cu[s] / 64 + s + c: ceil(len / 64) <= cu[s + 1] / 64 - cu[s] / 64 + 1,
-// so no two chunks share one and total / 64 + seqs slots are enough, without a prefix sum.
+// so no two chunks share one and total / 64 + seqs slots are enough, without a prefix sum.  (Of sequences
+// that start below no earlier bound: the others are taken as empty, so that rows and slots have one owner.)
 __host__ __device__ __forceinline__ int64_t gc_slots(int64_t seqs, int64_t total) { return total / GC_C + seqs; }
 
 struct GcArgs {
@@ -121,10 +122,11 @@ struct GcArgs {
     float scale;
     int l2norm;
     int parts;  // preparation blocks a (chunk, key head)
-    int* ready;  // [slot][value head]
+    int* ready;  // [slot][value head]; with the preparation before the recurrence the first says whether bounds are out of order
 };
 
-// Row bounds of a sequence; invalid ones make it empty.
+// Row bounds of a sequence; invalid ones make it empty.  That it starts below an earlier bound is for the callers
+// to find (gc_below).
 __device__ __forceinline__ int gc_bounds(const GcArgs& p, int seq, int& start) {
     if (!p.cu) {
         start = 0;
@@ -133,6 +135,14 @@ __device__ __forceinline__ int gc_bounds(const GcArgs& p, int seq, int& start) {
     start = p.cu[seq];
     const int end = p.cu[seq + 1];
     return (start < 0 || end > p.total || end < start) ? 0 : end - start;
+}
+
+// Whether a bound before sequence `seq` lies above its start: every `threads`-th bound from `i` on.  Asked only
+// where some bound is below the one before it.
+__device__ __forceinline__ bool gc_below(const int* cu, int seq, int start, int i, int threads) {
+    bool below = false;
+    for (; i < seq; i += threads) below |= cu[i] > start;
+    return below;
 }
 
 __device__ __forceinline__ int64_t gc_state_slot(const GcArgs& p, int seq) {
@@ -734,23 +744,28 @@ __global__ void __launch_bounds__(128, 5)
     // whose chunk this is
     pdl_wait();
     if (threadIdx.x == 0) {
-        sh.seq = -1;
+        sh.seq = p.seqs;
         mbar_init(&sh.full, 1);
         mbar_init(&sh.kqdone, 1);
         fence_barrier_init();
     }
     __syncthreads();
+    bool disordered = false;
     for (int s = threadIdx.x; s < p.seqs; s += 128) {
         int start;
         const int len = gc_bounds(p, s, start);
+        if (p.cu) disordered |= p.cu[s + 1] < start;
         const int64_t base = start / GC_C + s;
-        if (slot >= base && slot < base + (len + GC_C - 1) / GC_C && gc_state_slot(p, s) >= 0) sh.seq = s;
+        if (slot >= base && slot < base + (len + GC_C - 1) / GC_C && gc_state_slot(p, s) >= 0)
+            atomicMin(&sh.seq, s);  // (a later one with this slot starts below this one's end)
     }
-    __syncthreads();
+    disordered = __syncthreads_or(disordered);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.ready[0] = disordered;
     const int seq = sh.seq;
-    if (seq < 0) return;
+    if (seq == p.seqs) return;
     int start;
     const int len = gc_bounds(p, seq, start);
+    if (disordered && __syncthreads_or(gc_below(p.cu, seq, start, threadIdx.x, 128))) return;
     const int c = (int)(slot - (start / GC_C + seq));
     if (threadIdx.x < 32) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tslot)),
@@ -809,7 +824,7 @@ struct GcShared {
     uint32_t tslot;
     int failed;
     int seq;
-    int len[GC_MAX_SORT];
+    int len[GC_MAX_SORT];  // where chunks are prepared 0 for a sequence that starts below an earlier bound
 };
 constexpr size_t GC_SMEM = 1024 + 2 * GC_STAGE + 4 * GC_VTILE + sizeof(GcShared);
 static_assert(GC_SMEM <= 227 * 1024, "shared memory budget");
@@ -837,7 +852,7 @@ __device__ __forceinline__ bool gc_wait_ready(const int* flag) {
 
 // The chunks of all sequences, first chunks first, a value head at a time; `tb` and `smem` the CTA's.
 __device__ __forceinline__ bool gp_teams(const CUtensorMap* mapQ, const CUtensorMap* mapK, const GcArgs& p, uint8_t* smem,
-                                         uint32_t tb, int first, int workers) {
+                                         uint32_t tb, int first, int workers, const int* lens) {
     const int team = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 7), 0), bar = 1 + team;
     uint8_t* tile = smem + team * GP_TEAM;
     GpShared& sh = *reinterpret_cast<GpShared*>(tile + GC_KQ);
@@ -848,17 +863,22 @@ __device__ __forceinline__ bool gp_teams(const CUtensorMap* mapQ, const CUtensor
     }
     gp_sync(bar);
     const int group = p.hv / p.hk;
+    // (the lengths of several sequences with those that start below an earlier bound as 0)
+    auto bounds = [&](int s, int& start) {
+        const int len = gc_bounds(p, s, start);
+        return p.seqs > 1 ? min(len, lens[s]) : len;
+    };
     int most = 0;
     for (int s = 0; s < p.seqs; s++) {
         int start;
-        most = max(most, (gc_bounds(p, s, start) + GC_C - 1) / GC_C);
+        most = max(most, (bounds(s, start) + GC_C - 1) / GC_C);
     }
     const int64_t items = (int64_t)most * p.seqs * p.hv;
     uint32_t parity = 0;
     for (int64_t i = first + (int64_t)team * workers; i < items; i += 4 * (int64_t)workers) {
         const int head = (int)(i % p.hv), seq = (int)(i / p.hv % p.seqs), c = (int)(i / p.hv / p.seqs);
         int start;
-        const int len = gc_bounds(p, seq, start);
+        const int len = bounds(seq, start);
         if (GC_C * c >= len || gc_state_slot(p, seq) < 0) continue;
         const int64_t slot = start / GC_C + seq + c;
         const int kh = head / group;
@@ -925,11 +945,20 @@ __global__ void __launch_bounds__(GC_THREADS, 1)
     __syncthreads();
     gc_fence_after();
     // The longest sequences start first: a CTA takes the sequence of rank `order` by length.
+    bool disordered = !AHEAD && p.ready[0];  // (some bound is below the one before it)
     if (p.seqs > 1 && p.seqs <= GC_MAX_SORT) {
         const int i = threadIdx.x;
-        if (i < p.seqs) sh.len[i] = p.cu[i + 1] - p.cu[i];
-        __syncthreads();
-        if (i < p.seqs && !prepares) {
+        bool below = false;
+        if (i < p.seqs) {
+            const int len = p.cu[i + 1] - p.cu[i];
+            sh.len[i] = len;
+            below = len < 0;
+        }
+        if (AHEAD) disordered = __syncthreads_or(below);  // (at most half as many sequences as SMs)
+        else __syncthreads();
+        if (prepares) {
+            if (disordered && i < p.seqs && gc_below(p.cu, i, p.cu[i], 0, 1)) sh.len[i] = 0;
+        } else if (i < p.seqs) {
             const int len = sh.len[i];
             int rank = 0;
 #pragma unroll 8
@@ -947,15 +976,16 @@ __global__ void __launch_bounds__(GC_THREADS, 1)
     const int len = gc_bounds(p, seq, start);
     const int64_t slot = gc_state_slot(p, seq);
     const int n = slot >= 0 ? (len + GC_C - 1) / GC_C : 0;  // chunks
-    if (slot < 0 && len > 0 && !prepares) {                 // no state: the outputs are zero
+    const bool empty = disordered && __syncthreads_or(!prepares && gc_below(p.cu, seq, start, threadIdx.x, GC_THREADS));
+    if (slot < 0 && len > 0 && !prepares && !empty) {       // no state: the outputs are zero
         for (int i = threadIdx.x; i < len * (GC_D / 8); i += GC_THREADS)
             *reinterpret_cast<uint4*>(p.out + (((int64_t)start + i / (GC_D / 8)) * p.hv + head) * GC_D + 8 * (i % (GC_D / 8))) =
                 make_uint4(0, 0, 0, 0);
     }
 
     if (prepares) {
-        if (!gp_teams(&mapQ, &mapK, p, stages, tb, (int)blockIdx.x - p.seqs * p.hv, (int)gridDim.x - p.seqs * p.hv)) sh.failed = 1;
-    } else if (n == 0) {
+        if (!gp_teams(&mapQ, &mapK, p, stages, tb, (int)blockIdx.x - p.seqs * p.hv, (int)gridDim.x - p.seqs * p.hv, sh.len)) sh.failed = 1;
+    } else if (n == 0 || empty) {
         // nothing to do: the state stays as it is
     } else if (warp < GC_WOUT) {
         // ================================================================ the recurrence

@@ -277,8 +277,8 @@ int gated_delta_decode(const bq_heads* q, const bq_heads* k, const bq_heads* v, 
 
 /* Whole prompts: `total` token rows hold the sequences one after the other, sequence s the rows
  * cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device int32 [seqs + 1]; NULL: one sequence of all rows).  A
- * sequence may be empty (its state stays); bounds that are negative, past `total` or out of order make
- * the sequence empty.  Rows of no sequence keep their outputs.  Runs in chunks of 64 tokens on the
+ * sequence may be empty (its state stays); a bound that is negative, past `total` or below an earlier
+ * bound makes its sequences empty, so no two sequences share rows.  Rows of no sequence keep their outputs.  Runs in chunks of 64 tokens on the
  * tensor cores.  The state is fp32-accurate (every fp32 operand of its products is two scaled FP16 terms); the
  * products that only reach the BF16 outputs take one FP16 term of each operand, rounded to nearest: 2^-11 of
  * every term beside the outputs' own rounding.  A NaN or an infinity in a

@@ -131,3 +131,59 @@ def test_queries_that_are_stored_keys(B):
         assert np.all(np.abs(err) <= bf16_half_ulp(ref) * (1 + 2.0 ** -7) + 2.0 ** -11 * np.abs(ref)), what
         mean = (err * np.sign(ref)).sum() / np.abs(ref).sum()
         assert abs(mean) <= 2.0 ** -14, (what, np.log2(abs(mean)))
+
+
+def out_of_order(cu, total):
+    """The sequences that a list of bounds gives: bounds that are negative, past the end or below an
+    earlier one make theirs empty."""
+    spans, most = [], cu[0]
+    for a, b in zip(cu[:-1], cu[1:]):
+        good = 0 <= a <= b <= total and a >= most
+        spans.append((a, b) if good else (0, 0))
+        most = max(most, a, b)
+    return spans
+
+
+# one head: chunks prepared beside the recurrence; many heads, and more sequences than are ordered: before it
+@pytest.mark.parametrize("hk,hv", [(1, 1), (2, 32)])
+@pytest.mark.parametrize("cu", [[0, 200, 100, 300], [0, 130, 60, 190, 150, 300, 300], [0, 64, 500, 100, 300],
+                                [-5, 40, 20, 90, 300], [300, 0, 100, 300]])
+def test_bounds_out_of_order(B, cu, hk, hv):
+    total, n = 300, len(cu) - 1
+    a = make(31 + n, total, hk, hv, n)
+    spans = out_of_order(cu, total)
+    state, out = a[5].clone(), torch.full((total, hv, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.gated_delta_prefill(*a[:5], state, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), out=out)
+    torch.cuda.synchronize()
+    assert B.lib().bq_device_status() == 0
+    rest = torch.ones(total, dtype=torch.bool)
+    for s, (i, j) in enumerate(spans):
+        if i == j:
+            assert torch.equal(state[s], a[5][s]), s
+            continue
+        rest[i:j] = False
+        ref = reference(*(t[i:j] for t in a[:5]), a[5][s:s + 1], [j - i])
+        check(out[i:j], state[s:s + 1], ref, (cu, s))
+    assert (out.cpu()[rest] == 7).all()
+
+
+def test_bounds_out_of_order_among_many(B):
+    # 600 sequences, two of them with a bound that belongs elsewhere
+    lens = [1 + (i * 7) % 5 for i in range(600)]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    total = cu[-1]
+    cu[100], cu[500] = cu[100] - 40, cu[500] + 150
+    a = make(33, total, 1, 1, 600)
+    state, out = a[5].clone(), torch.full((total, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.gated_delta_prefill(*a[:5], state, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), out=out)
+    spans = out_of_order(cu, total)
+    assert 0 < sum(i == j for i, j in spans) < 300
+    rest = torch.ones(total, dtype=torch.bool)
+    for s, (i, j) in enumerate(spans):
+        if i == j:
+            assert torch.equal(state[s], a[5][s]), s
+            continue
+        rest[i:j] = False
+        ref = reference(*(t[i:j] for t in a[:5]), a[5][s:s + 1], [j - i])
+        check(out[i:j], state[s:s + 1], ref, s)
+    assert (out.cpu()[rest] == 7).all()
