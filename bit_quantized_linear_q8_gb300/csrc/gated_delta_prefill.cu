@@ -978,9 +978,9 @@ __global__ void __launch_bounds__(GC_THREADS, 1)
     const int n = slot >= 0 ? (len + GC_C - 1) / GC_C : 0;  // chunks
     const bool empty = disordered && __syncthreads_or(!prepares && gc_below(p.cu, seq, start, threadIdx.x, GC_THREADS));
     if (slot < 0 && len > 0 && !prepares && !empty) {       // no state: the outputs are zero
-        for (int i = threadIdx.x; i < len * (GC_D / 8); i += GC_THREADS)
-            *reinterpret_cast<uint4*>(p.out + (((int64_t)start + i / (GC_D / 8)) * p.hv + head) * GC_D + 8 * (i % (GC_D / 8))) =
-                make_uint4(0, 0, 0, 0);
+        uint4* row = reinterpret_cast<uint4*>(p.out + ((int64_t)start * p.hv + head) * GC_D) + threadIdx.x % (GC_D / 8);
+        for (int i = threadIdx.x / (GC_D / 8); i < len; i += GC_THREADS / (GC_D / 8))  // (16 threads a row)
+            row[(int64_t)i * p.hv * (GC_D / 8)] = make_uint4(0, 0, 0, 0);
     }
 
     if (prepares) {
