@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(256) int8_dequant_kernel(const uint8_t* __rest
         const int64_t at = 16 * i;
         int64_t row = at < (1ll << 32) ? (int64_t)((uint32_t)at / k) : at / k;
         uint32_t c = (uint32_t)(at - row * k);
-        if (at + 16 <= total && c + 16 <= k) {
+        if (at + 16 <= total && k - c >= 16) {  // (c + 16 could wrap)
             const uint4 w = ldg_nc128(codes + at);
             const float s = __ldg(scales + row);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};

@@ -1,4 +1,4 @@
-"""Lengths at which 32-bit counts would wrap: one sequence of 2^27 tokens."""
+"""Lengths at which 32-bit counts would wrap: one sequence of 2^27 tokens, rows of almost 2^32 codes."""
 import pytest
 import torch
 
@@ -42,3 +42,10 @@ def test_skipped_sequence_of_many_tokens(B, tokens):
     torch.cuda.synchronize()
     assert B.lib().bq_device_status() == 0
     assert all_equal(out[:tokens], 0.0) and (out[tokens:] == 7).all() and (state == 1).all()
+
+
+def test_dequant_int8_rows_of_almost_2_32(B):
+    k = 2 ** 32 - 8
+    codes = torch.ones((2, k), dtype=torch.int8, device="cuda")
+    out = B.dequant_int8_to_bf16(codes, torch.tensor([0.5, 2.0], device="cuda"))
+    assert all_equal(out[0], 0.5) and all_equal(out[1], 2.0)
