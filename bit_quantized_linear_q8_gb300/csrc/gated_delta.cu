@@ -182,7 +182,14 @@ int gd_check(const bq_heads* q, const bq_heads* k, const bq_heads* v, const bq_h
         if (h[i]->token_stride % 8 != 0 || h[i]->head_stride % 8 != 0 || h[i]->token_stride < 0 || h[i]->head_stride < 0)
             return fail(BQ_ERR_INVALID, "%s: strides of %c must be multiples of 8 and not negative", who, "qkv"[i]);
     }
-    if (!g->data || !beta->data) return fail(BQ_ERR_INVALID, "%s: g and beta must be non-NULL", who);
+    const bq_heads* f[2] = {g, beta};
+    for (int i = 0; i < 2; i++) {
+        const char* name = i ? "beta" : "g";
+        if (!f[i]->data || !aligned4(f[i]->data))
+            return fail(BQ_ERR_INVALID, "%s: %s must be non-NULL and 4-byte aligned", who, name);
+        if (f[i]->token_stride < 0 || f[i]->head_stride < 0)
+            return fail(BQ_ERR_INVALID, "%s: strides of %s must not be negative", who, name);
+    }
     if (!state || !aligned16(state) || !out || !aligned16(out))
         return fail(BQ_ERR_INVALID, "%s: state and out must be non-NULL and 16-byte aligned", who);
     if (slots > (1u << 30)) return fail(BQ_ERR_INVALID, "%s: too many slots", who);
@@ -201,6 +208,7 @@ extern "C" int gated_delta_decode(const bq_heads* q, const bq_heads* k, const bq
     if (batch == 0 || tokens == 0) return ok();
     const int st = gd_check(q, k, v, g, beta, state, out, heads_k, heads_v, head_dim, slots, who);
     if (st) return st;
+    if (!aligned4(state_idx)) return fail(BQ_ERR_INVALID, "%s: state_idx must be 4-byte aligned", who);
     if (!state_idx && slots < batch) return fail(BQ_ERR_INVALID, "%s: %u slots for a batch of %u", who, slots, batch);
     const uint64_t blocks = (uint64_t)batch * heads_v * (GD_D / GD_COLS);
     if (blocks >= (1ull << 31) || (uint64_t)batch * tokens >= (1ull << 31))

@@ -1411,6 +1411,8 @@ extern "C" int gated_delta_prefill(const bq_heads* q, const bq_heads* k, const b
     if (seqs == 0 || total == 0) return ok();
     int st = gd_check(q, k, v, g, beta, state, out, heads_k, heads_v, head_dim, slots, who);
     if (st) return st;
+    if (!aligned4(cu_seqlens) || !aligned4(state_idx))
+        return fail(BQ_ERR_INVALID, "%s: cu_seqlens and state_idx must be 4-byte aligned", who);
     if (!cu_seqlens && seqs != 1) return fail(BQ_ERR_INVALID, "%s: cu_seqlens is NULL for %u sequences", who, seqs);
     if (!state_idx && slots < seqs) return fail(BQ_ERR_INVALID, "%s: %u slots for %u sequences", who, slots, seqs);
     const uint64_t blocks = (uint64_t)gc_slots(seqs, total) * heads_k;

@@ -262,7 +262,8 @@ int int8_gemm(const int8_t* a, const float* sa, const int8_t* w, const float* sw
  * Source: init.rs, `Qwen3SsmLayer::new` (the layer that the qkv|z projection feeds). */
 
 /* A [tokens][heads][head_dim] tensor (or [tokens][heads] for g and beta) in elements: the last
- * dimension is contiguous.  q, k, v: data 16-byte aligned, strides multiples of 8; none negative. */
+ * dimension is contiguous.  q, k, v: data 16-byte aligned, strides multiples of 8; g, beta (and the index
+ * arrays): 4-byte aligned; no stride negative. */
 typedef struct bq_heads {
     const void* data;
     int64_t token_stride, head_stride;
