@@ -361,9 +361,13 @@ __global__ void __launch_bounds__(256) int8_dequant_kernel(const uint8_t* __rest
     }
 }
 
-static bool nq_overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && x < y + nb && y < x + na;
+struct NqRange {
+    const void* at;
+    size_t bytes;
+};
+static bool nq_overlap(const NqRange& a, const NqRange& b) {
+    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    return x && y && x < y + b.bytes && y < x + a.bytes;
 }
 
 // Checks shared by the norm and the row quantiser; kp and the scale plane are set for q8_1.
@@ -378,15 +382,22 @@ static int nq_run(NqArgs& p, bool norm, cudaStream_t stream, const char* who) {
             return fail(BQ_ERR_INVALID, "%s: weight must be non-NULL and 16-byte aligned", who);
         if (!aligned16(p.residual) || !aligned16(p.sum) || !aligned16(p.y))
             return fail(BQ_ERR_INVALID, "%s: residual, residual_out and y must be 16-byte aligned", who);
-        if (!(p.eps >= 0.0f)) return fail(BQ_ERR_INVALID, "%s: eps must not be negative", who);
         if (p.sum && !p.residual) return fail(BQ_ERR_INVALID, "%s: residual_out needs a residual", who);
-        // residual_out may be the residual or x themselves (every value's thread reads it first)
-        const size_t nb = (size_t)p.m * p.k * 2;
-        if ((p.sum != p.residual && nq_overlap(p.sum, nb, p.residual, nb)) || (p.sum != p.x && nq_overlap(p.sum, nb, p.x, nb)) ||
-            nq_overlap(p.sum, nb, p.y, nb) || nq_overlap(p.y, nb, p.x, nb) || nq_overlap(p.y, nb, p.residual, nb))
-            return fail(BQ_ERR_INVALID, "%s: outputs overlap each other or an input (residual_out may only be residual or x itself)",
-                        who);
     }
+    // residual_out may be the residual or x themselves (every value's thread reads it first); a row's codes
+    // would lie over other rows' values
+    const size_t nb = (size_t)p.m * p.k * 2;
+    const NqRange in[3] = {{p.x, nb}, {p.residual, nb}, {p.weight, (size_t)p.k * 2}};
+    const NqRange out[4] = {{p.sum, nb}, {p.y, nb}, {p.codes, (size_t)p.m * p.kp},
+                            {p.scales, FMT == NQ_INT8 ? (size_t)p.m * 4 : (size_t)p.m * (p.kp / 32) * 8}};
+    bool clash = false;
+    for (int i = 0; i < 4; i++) {
+        for (int j = 0; j < 3; j++) clash |= !(i == 0 && j < 2 && out[i].at == in[j].at) && nq_overlap(out[i], in[j]);
+        for (int j = 0; j < i; j++) clash |= nq_overlap(out[i], out[j]);
+    }
+    if (clash)
+        return fail(BQ_ERR_INVALID, "%s: outputs overlap each other or an input (residual_out may only be residual or x itself)", who);
+    if (!(p.eps >= 0.0f)) return fail(BQ_ERR_INVALID, "%s: eps must not be negative", who);
     return norm ? nq_launch<FMT, true>(p, stream, who) : nq_launch<FMT, false>(p, stream, who);
 }
 
@@ -423,6 +434,9 @@ extern "C" int dequant_int8_to_bf16(const int8_t* codes, const float* scales, ui
     if (!codes || !scales || !out || !aligned16(codes) || !aligned16(scales) || !aligned16(out))
         return fail(BQ_ERR_INVALID, "%s: codes, scales and out must be non-NULL and 16-byte aligned", who);
     const int64_t total = (int64_t)rows * k;
+    const NqRange to = {out, (size_t)total * 2};
+    if (nq_overlap(to, {codes, (size_t)total}) || nq_overlap(to, {scales, (size_t)rows * 4}))
+        return fail(BQ_ERR_INVALID, "%s: out overlaps an input", who);
     const int64_t want = ((total + 15) / 16 + 255) / 256, most = (int64_t)sm_count() * 64;
     return launch_programmatic(who, int8_dequant_kernel, (uint32_t)(want < most ? want : most), 256, 0, (cudaStream_t)stream,
                                (const uint8_t*)codes, scales, out, total, k);

@@ -214,7 +214,8 @@ int dequant_nvfp4_to_bf16(const void* packed, const void* scales, uint16_t* out,
  *   residual_out = BF16(h);  codes, scales from y.
  * x, residual, weight [k]: BF16.  residual may be NULL (h = x).  residual_out (needs a residual)
  * and y_out (BF16(y), for projections that stay in BF16) may be NULL; residual_out may be residual
- * or x themselves, other overlaps are BQ_ERR_INVALID.  Any m and k <= 2^24; all pointers
+ * or x themselves, any other overlap of an output (here and in the three calls below) with an input or
+ * another output is BQ_ERR_INVALID.  Any m and k <= 2^24; all pointers
  * 16-byte aligned; k = 0 is a no-op. */
 int rms_norm_int8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
                   uint16_t* residual_out, uint16_t* y_out, int8_t* codes, float* scales, uint32_t m, uint32_t k,

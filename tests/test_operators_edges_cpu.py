@@ -44,3 +44,24 @@ def test_gates_and_indices(L, which):
 def test_prefill_bounds_pointer(L):
     refused(L, delta(L, "prefill", cu=X + 1), b"cu_seqlens")
     refused(L, delta(L, "prefill"), b"scratch")
+
+
+def test_norm_overlaps(L):
+    # 4 x 64: x, residual, y and residual_out 512 bytes, weight 128, codes 256 (q8_1: 1024 and 256), scales 16
+    def norm(x=X, residual=2 * X, weight=3 * X, h=4 * X, y=5 * X, codes=6 * X, scales=7 * X, eps=-1.0):
+        return L.rms_norm_int8(P(x), P(residual), P(weight), eps, P(h), P(y), P(codes), P(scales), 4, 64, P(0))
+
+    for kw in (dict(codes=X + 496), dict(codes=2 * X + 16), dict(codes=3 * X + 112), dict(scales=X), dict(scales=3 * X + 112),
+               dict(codes=5 * X), dict(codes=4 * X + 256), dict(scales=6 * X + 240), dict(h=3 * X), dict(y=3 * X + 16),
+               dict(codes=X - 240), dict(h=X + 16), dict(h=5 * X)):
+        refused(L, norm(**kw), b"overlap")
+    # neighbours that only touch are no overlap: the call goes on to the next check
+    for kw in (dict(codes=X + 512), dict(codes=X - 256), dict(h=X), dict(h=2 * X), dict(scales=6 * X + 256)):
+        refused(L, norm(**kw), b"eps")
+    q8 = lambda act: L.rms_norm_q8_1(P(X), P(0), P(3 * X), 1e-6, P(0), P(0), P(act), 4, 64, P(0))  # noqa: E731
+    refused(L, q8(X + 16), b"overlap")
+    refused(L, q8(X - 1024 - 16), b"overlap")  # the scales behind the codes
+    refused(L, L.quantize_int8(P(X), P(X), P(7 * X), 4, 64, P(0)), b"overlap")
+    refused(L, L.quantize_int8(P(X), P(6 * X), P(6 * X), 4, 64, P(0)), b"overlap")
+    refused(L, L.dequant_int8_to_bf16(P(X), P(3 * X), P(X - 16), 4, 64, P(0)), b"overlap")
+    refused(L, L.dequant_int8_to_bf16(P(X), P(3 * X), P(3 * X - 16), 4, 64, P(0)), b"overlap")
