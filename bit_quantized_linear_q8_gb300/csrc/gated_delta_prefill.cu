@@ -1470,8 +1470,10 @@ extern "C" int gated_delta_prefill(const bq_heads* q, const bq_heads* k, const b
         cfg.attrs = at;
         cfg.numAttrs = 1;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, gated_delta_recur_kernel<true>, map[0], map[1], map[2], a);
-        if (e != cudaSuccess) return fail(BQ_ERR_LAUNCH, "%s: %s", who, cudaGetErrorString(e));
-        return check_launch(who);
+        if (e == cudaSuccess) return check_launch(who);
+        cudaGetLastError();
+        // (a process that holds a part of the device cannot have a CTA on every SM at once: the two kernels below)
+        if (e != cudaErrorCooperativeLaunchTooLarge) return fail(BQ_ERR_LAUNCH, "%s: %s", who, cudaGetErrorString(e));
     }
     // A block for every value head while all of them run at once (64 tokens x 48 heads: 20.7 us, 26.9 with
     // one a key head), else one a key head, which forms [K; Q] K^T once for its value heads (8192 x 48:
