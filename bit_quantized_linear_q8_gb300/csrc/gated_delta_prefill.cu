@@ -19,16 +19,16 @@
 //  * Many chains (pairs of a sequence and a value head): two kernels, the preparation on all SMs, five
 //    blocks of one chunk each an SM, then the recurrence.
 //  * Up to half as many chains as SMs: one launch, in which the SMs without a chain prepare the
-//    chunks in the order of the chains' need and raise a flag for each (8192 tokens x 48 heads: 340 us,
+//    chunks in the order of the chains' need and raise a flag for each (8192 tokens x 48 heads: 342 us,
 //    428 with two kernels; 2048 x 48: 106 and 124 us; but 2 sequences, 700 + 300 tokens, x 48: 75 and 57
 //    us, the remaining 56 SMs being too few).  A cooperative launch, one CTA an SM: the CTAs that are
 //    waited for run.
 // (Four warps in the recurrence's own CTA that prepared its next chunk took 811 us for 8192 x 48: a chunk
 // of preparation is longer than one of recurrence.)
 // Bound: the recurrence by its chain, about 4600 cycles a chunk: three dependent products (S K^T, T R, V''
-// K; 2500 cycles of MMAs) and the conversions between them, which the SM's four schedulers run at
-// half of their issue rate; the preparation by its barriers and instruction issue (98 us for 8192 x 48
-// on all SMs).
+// K; 2500 cycles of MMAs) and the conversions between them (over a launch a third of the SMs' issue slots
+// and a fifth of the tensor pipe are used); the preparation by its barriers and the shared memory's latency (98 us for
+// 8192 x 48 on all SMs).
 //
 // Precision.  All products run in the FP16 kind.  A row of K or Q is scaled by a power of two to
 // below 2^8 and its BF16 values (8 bits) are then FP16 values exactly (down to 2^-25 of the row's

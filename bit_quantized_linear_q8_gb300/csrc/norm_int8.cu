@@ -10,10 +10,13 @@
 //
 // The row stays in registers between its two reductions (sum of squares, maximum), so each
 // value is read once and written once: 7 bytes a value with a residual (x, residual, sum and
-// code), 3 without.  Bound: HBM for large m with a residual (4096 x 5120: 25.3 us, 5.8 TB/s),
-// instruction issue without one (2048 x 6144: 13.1 us), the launch and the two block reductions' latency
-// for few rows (4 x 5120: 2.8 us).  Packed arithmetic and a division decided once a row took 4096 x 5120
-// from 38.3 to 28.8 us; all kernels here are launched programmatically, which takes 1.4-3.6 us off each.
+// code), 3 without.  Bound: HBM for large m with a residual (4096 x 5120: 24.9 us, 5.9 TB/s), latency
+// without one (2048 x 6144: 11.9 us, the row quantiser 8.4, their bytes 5.6: one row a block, its load, two
+// block reductions and its store one after the other; 43 % of the issue slots are used), the launch and the
+// reductions' latency for few rows (4 x 5120: 2.6 us).  The q8_1 output: 27.3 us for 4096 x 5120 with a
+// residual, 13.8 for 2048 x 6144 without.  (All of these from a graph.)  Packed arithmetic and a division
+// decided once a row took 4096 x 5120 from 38.3 to 28.8 us; all kernels here are launched
+// programmatically, which takes 1.4-3.6 us off each.
 // (Streaming loads or stores change nothing or lose 1 us.)
 #include "common.cuh"
 

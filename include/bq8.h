@@ -241,7 +241,7 @@ size_t bq_int8_gemm_scratch_bytes(uint32_t m, uint32_t n, uint32_t k);
 /* W8A8 product: out[m][n] = BF16(sa[m] sw[n] sum_k a[m][k] w[n][k]); a [m][k], w [n][k] int8.
  * The products are exact and the sums fp32: exact integers while |sum| < 2^24, rounded beyond.
  * k % 16 == 0 (else BQ_ERR_INVALID); any m and n; scratch: bq_int8_gemm_scratch_bytes(m, n, k)
- * bytes, NULL when that is 0.  m = 0 or n = 0 is a no-op, k = 0 writes zeros.  A failed internal
+ * bytes on the launching GPU, NULL when that is 0; out and scratch overlap no other tensor of the call.  m = 0 or n = 0 is a no-op, k = 0 writes zeros.  A failed internal
  * wait is reported by bq_device_status.
  * Source: w8a8_decode.rs (the W8A8 arm of the qkv|z and output projections). */
 int int8_gemm(const int8_t* a, const float* sa, const int8_t* w, const float* sw, uint16_t* out, void* scratch,
@@ -252,12 +252,14 @@ int int8_gemm(const int8_t* a, const float* sa, const int8_t* w, const float* sw
  * Per value head h with state S [128 (key)][128 (value)] fp32, for the tokens of a sequence in order:
  *   S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q
  * Query and key heads are shared by heads_v / heads_k consecutive value heads.  With l2norm, q and
- * k are first divided by sqrt(sum of squares + 1e-6).
+ * k are first divided by sqrt(sum of squares + 1e-6) (a row whose sum of squares leaves fp32, a norm above 1.8e19,
+ * reads as zeros).
  *   q, k [tokens][heads_k][128], v [tokens][heads_v][128]: BF16, g (log decay) and beta
  *   [tokens][heads_v]: fp32, all with strides (so the sections of a fused projection's rows need
  *   no copy); state [slots][heads_v][128][128] fp32, updated in place; out [tokens][heads_v][128]
  *   BF16, contiguous.
- * g may be -infinity (the state is forgotten) but not +infinity.  state_idx[s] is the slot of sequence s (NULL: slot
+ * g may be -infinity (a finite state is forgotten; NaN and infinity stay) but not +infinity.  out overlaps no
+ * other tensor of the call.  state_idx[s] is the slot of sequence s (NULL: slot
  * s); a sequence whose slot is negative or >= slots is skipped, its outputs are zero.  Two sequences
  * of one call must not share a slot.
  * Source: init.rs, `Qwen3SsmLayer::new` (the layer that the qkv|z projection feeds). */
