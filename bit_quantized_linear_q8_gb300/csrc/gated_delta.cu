@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(128) gated_delta_decode_kernel(const GdArgs p)
             sk.z += x.z;
             sk.w += x.w;
         }
+        // (a state that is forgotten counts as zeros: its products may have left fp32, and 0 times infinity is not 0)
+        if (a == 0.0f) sk = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const float ark = a * rk;
         const float4 u = make_float4(b * (vv[0] - ark * sk.x), b * (vv[1] - ark * sk.y), b * (vv[2] - ark * sk.z),
                                      b * (vv[3] - ark * sk.w));
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(128) gated_delta_decode_kernel(const GdArgs p)
                 sq.z += x.z;
                 sq.w += x.w;
             }
+            if (a == 0.0f) sq = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             const float c = qk * rk;
             *reinterpret_cast<uint2*>(p.out + (tok * p.hv + head) * GD_D + col) =
                 make_uint2(bf162_bits(__floats2bfloat162_rn(rq * fmaf(a, sq.x, c * u.x), rq * fmaf(a, sq.y, c * u.y))),

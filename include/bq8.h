@@ -258,7 +258,7 @@ int int8_gemm(const int8_t* a, const float* sa, const int8_t* w, const float* sw
  *   [tokens][heads_v]: fp32, all with strides (so the sections of a fused projection's rows need
  *   no copy); state [slots][heads_v][128][128] fp32, updated in place; out [tokens][heads_v][128]
  *   BF16, contiguous.
- * g may be -infinity (a finite state is forgotten; NaN and infinity stay) but not +infinity.  out overlaps no
+ * g may be -infinity (a finite state is forgotten) but not +infinity.  out overlaps no
  * other tensor of the call.  state_idx[s] is the slot of sequence s (NULL: slot
  * s); a sequence whose slot is negative or >= slots is skipped, its outputs are zero.  Two sequences
  * of one call must not share a slot.

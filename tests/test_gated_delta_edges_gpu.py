@@ -63,6 +63,24 @@ def test_large_state_is_forgotten(B, size, tokens, forget):
         assert not s[0, 1].any() and not s[0, 0, :, 3:9].any(), what
 
 
+@pytest.mark.parametrize("tokens", [1, 65])
+def test_largest_state_is_forgotten(B, tokens):
+    # Products with such a state leave fp32, and nothing of them may stay: what comes out is what comes from a
+    # state of zeros.  Scales by powers of two do not change how terms are rounded, so the states agree as
+    # closely as fp32 sums do and the outputs to a BF16 neighbour.
+    q, k, v, g, beta, state = make(tokens + 2, tokens, 1, 2, 1)
+    q, k = q.abs(), k.abs()
+    g[0] = float("-inf")
+    state.fill_(3e38)
+    zeros = torch.zeros_like(state)
+    mag = reference(q, k, v, g, beta, zeros, [tokens])[2].cuda()
+    args = (q, k, v, g, beta)
+    for (what, out, s), (_, out0, s0) in zip(both_forms(B, args, state, tokens), both_forms(B, args, zeros, tokens)):
+        assert bool(((s - s0).abs() <= 2.0 ** -17 * mag[:, None, None]).all()), what
+        limit = 2.0 ** -7 * out0.float().abs() + 2.0 ** -17 * mag[:, None]
+        assert bool(((out.float() - out0.float()).abs() <= limit).all()), what
+
+
 def test_large_state_forgotten_in_mid_prompt(B):
     # a chunk that writes nothing, then one that forgets, then ordinary ones; compared with a start from zeros there
     q, k, v, g, beta, state = make(9, 300, 1, 2, 1)
